@@ -5,6 +5,10 @@ takes CUDA tensors, checks dtype / device / contiguity / shape, passes raw devic
 pointers and sizes across the C ABI and raises ``CQError`` on a non-OK status.  All
 arithmetic runs in the library's CUDA kernels; there is no fallback of any kind: if
 the shared library is missing or does not load, every call raises.
+
+``stream`` (a ``torch.cuda.Stream`` or a raw handle) is where a call launches, the current
+stream by default.  Outputs and workspaces that the call allocates come from that stream's
+memory, as if it were the current one.
 """
 
 import ctypes
@@ -134,6 +138,19 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """``torch.empty`` for what a call launched on ``stream`` allocates.  Memory of the current
+    stream's pool would not do for another one: work queued there may still use the block, and
+    a workspace dropped on return would be handed out again before the kernels have run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # ExternalStream(0) would be a new stream
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ptr(t, dtype, name, ndim=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -189,7 +206,7 @@ def cq_codebook_fit(samples, L, iters=200, levels_out=None, stream=None):
     """A1: Lloyd-Max levels (float32 [L]) from float64 samples on the GPU."""
     s = _ptr(samples, torch.float64, "samples")
     if levels_out is None:
-        levels_out = torch.empty(L, dtype=torch.float32, device=samples.device)
+        levels_out = _empty(L, torch.float32, samples.device, stream)
     _check("cq_codebook_fit", lib().cq_codebook_fit(s, samples.numel(), L, iters,
                                                      _ptr(levels_out, torch.float32, "levels_out"),
                                                      _stream(stream)))
@@ -212,9 +229,9 @@ def cq_encode(W, b, cb, packed=None, norms=None, g=128, stream=None):
     N, K = W.shape
     wp = _ptr(W, torch.float32, "W", 2)
     if packed is None:
-        packed = torch.empty((N, K // 128, 16 * cq_field_bits(b)), dtype=torch.uint8, device=W.device)
+        packed = _empty((N, K // 128, 16 * cq_field_bits(b)), torch.uint8, W.device, stream)
     if norms is None:
-        norms = torch.empty((N, K // 128), dtype=torch.int16, device=W.device)
+        norms = _empty((N, K // 128), torch.int16, W.device, stream)
     c = _cbk(cb)
     _check("cq_encode", lib().cq_encode(wp, N, K, g, b, ctypes.byref(c),
                                         _ptr(packed, torch.uint8, "packed"),
@@ -227,9 +244,9 @@ def a8_quantize(X, Xq=None, scale=None, stream=None):
     B, K = X.shape
     xp = _ptr(X, torch.float32, "X", 2)
     if Xq is None:
-        Xq = torch.empty((B, K), dtype=torch.int8, device=X.device)
+        Xq = _empty((B, K), torch.int8, X.device, stream)
     if scale is None:
-        scale = torch.empty((B,), dtype=torch.float32, device=X.device)
+        scale = _empty((B,), torch.float32, X.device, stream)
     _check("a8_quantize", lib().a8_quantize(xp, B, K, _ptr(Xq, torch.int8, "Xq"),
                                             _ptr(scale, torch.float32, "scale"), _stream(stream)))
     return Xq, scale
@@ -239,9 +256,9 @@ def a8_quantize_groups(X, G, codes=None, scales=None, stream=None):
     """Grouped A8: X [T, D] float32 -> (codes int8 [T, D], scales float32 [T, D/G])."""
     T, D = X.shape
     if codes is None:
-        codes = torch.empty((T, D), dtype=torch.int8, device=X.device)
+        codes = _empty((T, D), torch.int8, X.device, stream)
     if scales is None:
-        scales = torch.empty((T, D // G), dtype=torch.float32, device=X.device)
+        scales = _empty((T, D // G), torch.float32, X.device, stream)
     _check("a8_quantize_groups", lib().a8_quantize_groups(_ptr(X, torch.float32, "X", 2), T, D, G,
                                                           _ptr(codes, torch.int8, "codes"),
                                                           _ptr(scales, torch.float32, "scales"),
@@ -253,7 +270,7 @@ def a8_fake_quant_groups(X, G, Y=None, stream=None):
     """Grouped A8 fake-quant: Y [T, D] float32 = q * s per group of G features."""
     T, D = X.shape
     if Y is None:
-        Y = torch.empty((T, D), dtype=torch.float32, device=X.device)
+        Y = _empty((T, D), torch.float32, X.device, stream)
     _check("a8_fake_quant_groups", lib().a8_fake_quant_groups(_ptr(X, torch.float32, "X", 2), T, D, G,
                                                               _ptr(Y, torch.float32, "Y"), _stream(stream)))
     return Y
@@ -267,10 +284,10 @@ def cq_gemv(packed, norms, N, K, b, cb, Xq, scale, Y=None, workspace=None, g=128
     """A4+A5: Y [B, N] float32 = decode GEMV of CQ weights with int8 activations."""
     B = Xq.shape[0]
     if Y is None:
-        Y = torch.empty((B, N), dtype=torch.float32, device=Xq.device)
+        Y = _empty((B, N), torch.float32, Xq.device, stream)
     need = cq_gemv_workspace_bytes(B, K)
     if workspace is None:
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=Xq.device)
+        workspace = _empty((max(need, 16),), torch.uint8, Xq.device, stream)
     c = _cbk(cb)
     _check("cq_gemv", lib().cq_gemv(_ptr(packed, torch.uint8, "packed"),
                                     _ptr(norms, torch.int16, "norms"), N, K, g, b, ctypes.byref(c),
@@ -285,7 +302,7 @@ def cq_gemv_lut(packed, norms, N, K, b, cb, Xq, scale, Y=None, g=128, stream=Non
     """A4+A5 by table lookup (b = 1, 2 or ternary): Y [B, N] float32, no workspace."""
     B = Xq.shape[0]
     if Y is None:
-        Y = torch.empty((B, N), dtype=torch.float32, device=Xq.device)
+        Y = _empty((B, N), torch.float32, Xq.device, stream)
     c = _cbk(cb)
     _check("cq_gemv_lut", lib().cq_gemv_lut(_ptr(packed, torch.uint8, "packed"),
                                             _ptr(norms, torch.int16, "norms"), N, K, g, b,
@@ -303,10 +320,10 @@ def cq_gemm(packed, norms, N, K, b, cb, Xq, scale, Y=None, workspace=None, g=128
     """A4+A6: Y [M, N] bfloat16 = prefill GEMM of CQ weights with int8 activations."""
     M = Xq.shape[0]
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=Xq.device)
+        Y = _empty((M, N), torch.bfloat16, Xq.device, stream)
     need = cq_gemm_workspace_bytes(M, K)
     if workspace is None:
-        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=Xq.device)
+        workspace = _empty((max(need, 256),), torch.uint8, Xq.device, stream)
     c = _cbk(cb)
     _check("cq_gemm", lib().cq_gemm(_ptr(packed, torch.uint8, "packed"),
                                     _ptr(norms, torch.int16, "norms"), N, K, g, b, ctypes.byref(c),
@@ -385,8 +402,7 @@ def cq_gemm_grouped(problems, M, b, cb, workspace=None, g=128, stream=None, devi
     """A6 grouped: every problem (a ``cq_gemm_problem`` array) in persistent launches."""
     need = cq_gemm_grouped_workspace_bytes(problems, M)
     if workspace is None:
-        workspace = torch.empty((max(need, 256),), dtype=torch.uint8,
-                                device=device or torch.device("cuda"))
+        workspace = _empty((max(need, 256),), torch.uint8, device or torch.device("cuda"), stream)
     c = _cbk(cb)
     _check("cq_gemm_grouped", lib().cq_gemm_grouped(problems, len(problems), M, g, b,
                                                     ctypes.byref(c),
@@ -415,7 +431,7 @@ def cq_gemv_noalloc(packed, norms, N, K, b, cb, Xq, scale, Y=None, g=128, stream
     stream capture.  ``Y`` may be passed preallocated."""
     B = Xq.shape[0]
     if Y is None:
-        Y = torch.empty((B, N), dtype=torch.float32, device=Xq.device)
+        Y = _empty((B, N), torch.float32, Xq.device, stream)
     c = _cbk(cb)
     _check("cq_gemv_noalloc", lib().cq_gemv_noalloc(
         _ptr(packed, torch.uint8, "packed"), _ptr(norms, torch.int16, "norms"), N, K, g, b,
@@ -428,7 +444,7 @@ def q4_0_quantize(W, blocks=None, stream=None):
     """A7: W [N, K] float32 -> Q4_0 blocks uint8 [N, ceil(K/32)*18]."""
     N, K = W.shape
     if blocks is None:
-        blocks = torch.empty((N, ((K + 31) // 32) * 18), dtype=torch.uint8, device=W.device)
+        blocks = _empty((N, ((K + 31) // 32) * 18), torch.uint8, W.device, stream)
     _check("q4_0_quantize", lib().q4_0_quantize(_ptr(W, torch.float32, "W", 2), N, K,
                                                 _ptr(blocks, torch.uint8, "blocks"), _stream(stream)))
     return blocks
@@ -438,7 +454,7 @@ def q4_0_gemv(blocks, N, K, X, Y=None, stream=None):
     """A8: Y [B, N] float32 = Q4_0 decode GEMV with float32 activations X [B, K]."""
     B = X.shape[0]
     if Y is None:
-        Y = torch.empty((B, N), dtype=torch.float32, device=X.device)
+        Y = _empty((B, N), torch.float32, X.device, stream)
     _check("q4_0_gemv", lib().q4_0_gemv(_ptr(blocks, torch.uint8, "blocks"), N, K,
                                         _ptr(X, torch.float32, "X"), B, _ptr(Y, torch.float32, "Y"),
                                         _stream(stream)))
@@ -454,10 +470,10 @@ def q4_0_gemm(blocks, N, K, X, Y=None, workspace=None, stream=None):
     (ceil(K/32) a multiple of 8)."""
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _empty((M, N), torch.float32, X.device, stream)
     need = q4_0_gemm_workspace_bytes(M, K)
     if workspace is None:
-        workspace = torch.empty((max(need, 256),), dtype=torch.uint8, device=X.device)
+        workspace = _empty((max(need, 256),), torch.uint8, X.device, stream)
     _check("q4_0_gemm", lib().q4_0_gemm(_ptr(blocks, torch.uint8, "blocks"), N, K,
                                         _ptr(X, torch.float32, "X"), M, _ptr(Y, torch.float32, "Y"),
                                         _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
@@ -532,14 +548,14 @@ def f8_quantize(X, rows=None, codes=None, scales=None, workspace=None, stream=No
         rp = _at(rows, _I32, shape, "rows")
         if workspace is None and R * K >= 1 << 20:   # smaller gathers take none
             need = f8_quantize_workspace_bytes(M, K, R)
-            workspace = torch.empty((need,), dtype=_U8, device=X.device) if need else None
+            workspace = _empty((need,), _U8, X.device, stream) if need else None
         if workspace is not None:
             wp, wn = _ptr(workspace, _U8, "workspace"), workspace.numel()
     cs, ss = (R, (K + 127) // 128 * 128), (R, (K + 511) // 512 * 4)
     if codes is None:
-        codes = torch.empty(cs, dtype=_U8, device=X.device)
+        codes = _empty(cs, _U8, X.device, stream)
     if scales is None:
-        scales = torch.empty(ss, dtype=_U8, device=X.device)
+        scales = _empty(ss, _U8, X.device, stream)
     status = (_lib or lib()).f8_quantize(
         xp, xt, M, K, rp, R, _at(codes, _U8, cs, "codes"), _at(scales, _U8, ss, "scales"), wp, wn,
         _raw_stream(X.get_device()) if stream is None else _stream(stream))
@@ -558,9 +574,9 @@ def f8_quantize_weights(W, codes=None, scales=None, stream=None):
     cs = (*lead, N, f8_row_bytes(K))
     ss = (*lead, (N + F8_GROUP - 1) // F8_GROUP, f8_scale_bytes(K))
     if codes is None:
-        codes = torch.empty(cs, dtype=_U8, device=W.device)
+        codes = _empty(cs, _U8, W.device, stream)
     if scales is None:
-        scales = torch.empty(ss, dtype=_U8, device=W.device)
+        scales = _empty(ss, _U8, W.device, stream)
     _check("f8_quantize_weights", lib().f8_quantize_weights(
         wp, wt, lead[0] if lead else 1, N, K, _at(codes, _U8, cs, "codes"), _at(scales, _U8, ss, "scales"),
         _raw_stream(W.get_device()) if stream is None else _stream(stream)))
@@ -583,7 +599,7 @@ def f8_gemm(wcodes, wscales, N, K, xcodes, xscales, act="none", Y=None, stream=N
     a, M = _gated(act), _dims(xcodes, "xcodes", 2)[0]
     Kp, Ks, shape = (K + 127) // 128 * 128, (K + 511) // 512 * 4, (M, N >> a)
     if Y is None:
-        Y = torch.empty(shape, dtype=_BF16, device=xcodes.device)
+        Y = _empty(shape, _BF16, xcodes.device, stream)
     yt = _float(Y, "Y")
     status = (_lib or lib()).f8_gemm(
         _at(wcodes, _U8, (N, Kp), "wcodes"), _at(wscales, _U8, ((N + 127) // 128, Ks), "wscales"), N, K,
@@ -601,7 +617,7 @@ def f8_gemm_experts(wcodes, wscales, N, K, offsets, xcodes, xscales, act="none",
     E = _dims(offsets, "offsets", 1)[0] - 1
     Kp, Ks, shape = (K + 127) // 128 * 128, (K + 511) // 512 * 4, (R, N >> a)
     if Y is None:
-        Y = torch.empty(shape, dtype=_BF16, device=xcodes.device)
+        Y = _empty(shape, _BF16, xcodes.device, stream)
     yt = _float(Y, "Y")
     status = (_lib or lib()).f8_gemm_experts(
         _at(wcodes, _U8, (E, N, Kp), "wcodes"), _at(wscales, _U8, (E, (N + 127) // 128, Ks), "wscales"), E, N, K,
@@ -623,17 +639,16 @@ def moe_route(logits, k, normalize=True, workspace=None, stream=None):
     ``moe_combine``).  ``normalize``: the weights sum to 1 over the k chosen, else over E."""
     T, E = shape = _dims(logits, "logits", 2)
     lp = _at(logits, _F32, shape, "logits")
-    dev, empty, l = logits.device, torch.empty, _lib or lib()
+    dev, l = logits.device, _lib or lib()
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _ptr(workspace, _U8, "workspace"), workspace.numel()
     elif T > MOE_ONE_LAUNCH:
         wn = l.moe_route_workspace_bytes(T, E)
-        workspace = empty((wn,), dtype=_U8, device=dev)
+        workspace = _empty((wn,), _U8, dev, stream)
         wp = workspace.data_ptr()
-    ids, weights = empty((T, k), dtype=_I32, device=dev), empty((T, k), dtype=_F32, device=dev)
-    rows, offsets = empty((T * k,), dtype=_I32, device=dev), empty((E + 1,), dtype=_I32, device=dev)
-    pos = torch.empty_like(ids)
+    ids, weights, pos = _empty((T, k), _I32, dev, stream), _empty((T, k), _F32, dev, stream), _empty((T, k), _I32, dev, stream)
+    rows, offsets = _empty((T * k,), _I32, dev, stream), _empty((E + 1,), _I32, dev, stream)
     status = l.moe_route(lp, T, E, k, 1 if normalize else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
                          rows.data_ptr(), pos.data_ptr(), wp, wn,
                          _raw_stream(logits.get_device()) if stream is None else _stream(stream))
@@ -649,7 +664,7 @@ def moe_combine(Y, pos, weights, out=None, stream=None):
     R, N = ys = _dims(Y, "Y", 2)
     T, k = ps = _dims(pos, "pos", 2)
     if out is None:
-        out = torch.empty((T, N), dtype=Y.dtype, device=Y.device)
+        out = _empty((T, N), Y.dtype, Y.device, stream)
     ot = _float(out, "out")
     status = (_lib or lib()).moe_combine(
         _at(Y, Y.dtype, ys, "Y"), yt, R, N, _at(pos, _I32, ps, "pos"), _at(weights, _F32, ps, "weights"), T, k,
