@@ -138,16 +138,22 @@ def _stream(stream):
     return ctypes.c_void_p(int(stream))
 
 
-def _empty(shape, dtype, device, stream):
-    """``torch.empty`` for what a call launched on ``stream`` allocates.  Memory of the current
-    stream's pool would not do for another one: work queued there may still use the block, and
-    a workspace dropped on return would be handed out again before the kernels have run."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _on(stream, device):
+    """The context in which what a call launched on ``stream`` allocates is that stream's memory.
+    Memory of the current stream's pool would not do for another one: work queued there may
+    still use the block, and a workspace dropped on return would be handed out again before
+    the kernels have run."""
     if not isinstance(stream, torch.cuda.Stream):
         # ExternalStream(0) would be a new stream
         stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    """``torch.empty`` for a call launched on ``stream``."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -639,19 +645,22 @@ def moe_route(logits, k, normalize=True, workspace=None, stream=None):
     ``moe_combine``).  ``normalize``: the weights sum to 1 over the k chosen, else over E."""
     T, E = shape = _dims(logits, "logits", 2)
     lp = _at(logits, _F32, shape, "logits")
-    dev, l = logits.device, _lib or lib()
+    if stream is not None:
+        with _on(stream, logits.device):
+            return moe_route(logits, k, normalize, workspace)
+    dev, empty, l = logits.device, torch.empty, _lib or lib()
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _ptr(workspace, _U8, "workspace"), workspace.numel()
     elif T > MOE_ONE_LAUNCH:
         wn = l.moe_route_workspace_bytes(T, E)
-        workspace = _empty((wn,), _U8, dev, stream)
+        workspace = empty((wn,), dtype=_U8, device=dev)
         wp = workspace.data_ptr()
-    ids, weights, pos = _empty((T, k), _I32, dev, stream), _empty((T, k), _F32, dev, stream), _empty((T, k), _I32, dev, stream)
-    rows, offsets = _empty((T * k,), _I32, dev, stream), _empty((E + 1,), _I32, dev, stream)
+    ids, weights = empty((T, k), dtype=_I32, device=dev), empty((T, k), dtype=_F32, device=dev)
+    rows, offsets = empty((T * k,), dtype=_I32, device=dev), empty((E + 1,), dtype=_I32, device=dev)
+    pos = empty((T, k), dtype=_I32, device=dev)
     status = l.moe_route(lp, T, E, k, 1 if normalize else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                         rows.data_ptr(), pos.data_ptr(), wp, wn,
-                         _raw_stream(logits.get_device()) if stream is None else _stream(stream))
+                         rows.data_ptr(), pos.data_ptr(), wp, wn, _raw_stream(logits.get_device()))
     if status:
         _check("moe_route", status)
     return ids, weights, offsets, rows, pos
