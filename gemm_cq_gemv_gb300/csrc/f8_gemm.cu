@@ -24,8 +24,9 @@
 //               each); allocates tensor memory
 // Tensor memory: two fp32 accumulators of BT columns (the epilogue of a tile overlaps the
 // next main loop), then a few buffers of scale words.
-// Every mbarrier wait is bounded; on expiry the CTA raises the device error word, waits for
-// what it has in flight (again bounded), frees its tensor memory and returns.
+// Every mbarrier wait is bounded, and begins after the dependent-launch wait: it never counts the
+// time of the kernel before.  On expiry the CTA raises the device error word, waits for what
+// it has in flight (again bounded), frees its tensor memory and returns.
 //
 // What bounds it, measured on one GB300:
 //   few tokens   the weights' bytes: 1x128256x4096 78 us (6.7 TB/s, the copy rate), 1x8192x28672
@@ -557,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
     const int k1 = kSplit ? (int)((int64_t)p.kb * (rank + 1) / (uint32_t)size) : p.kb;
     // where its run `seg` of them begins
     auto run_begin = [&](int seg) { return k0 + (int)((int64_t)(k1 - k0) * seg / p.segs); };
+    int issued = 0;   // stages that this thread has issued copies for (copy warp)
 
     if (warp < kEpiWarps) {
         // ------------------------------ epilogue ----------------------------------
@@ -744,9 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
     } else if (warp == kCopyWarp) {
         // ------------------------------ copies ------------------------------------
         if (elect_lane()) {
-            int s = 0, issued = 0;
+            int s = 0;
             uint32_t ph = 0;
-            bool ok = true;
             // one stage: the weight rows, and this CTA's token rows, all of the tile's or its half
             // of them (rounded to the MMA's N); whole boxes, rows past the tile are not used
             auto boxes_of = [&](const F8Tile& t) {
@@ -777,21 +778,15 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
             }
             while (any) {
                 for (; k < k1; ++k) {
-                    if (!wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                    if (!wait(&empty[s], ph ^ 1u)) break;
                     copy_w(t, k, s);
                     copy_x(t, k, s);
                     ++issued;
                     if (++s == kStages) { s = 0; ph ^= 1u; }
                 }
-                if (!ok) break;
+                if (k < k1) break;
                 k = k0;
                 any = walk.next(t);
-            }
-            if (!ok && (rank == 0 || !kPair)) {   // the copies in flight land before the memory is given back
-                volatile int none = 0;
-                for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-                    (void)mbar_wait_until<kCluster>(&full[i % kStages], (uint32_t)((i / kStages) & 1), &none, p.err,
-                                                    100000000ull);
             }
         }
         __syncwarp();
@@ -800,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
         // elect.sync, not a test of the lane: the compiler then keeps the operands in uniform
         // registers (four MMAs issue in 60 cycles instead of 316)
         if ((rank == 0 || !kPair) && elect_lane()) {
+            if constexpr (!C::EXPERTS) pdl_wait();   // its inputs come no sooner, and its waits are bounded
             int s = 0, g = 0;   // stage, group of scale words
             uint32_t ph = 0, sa = 0;
             bool ok = true;
@@ -854,19 +850,27 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
                 }
                 if (ok) commit<kPair>(&acc_full[buf]);
             }
-            if (!ok) {   // every MMA issued so far completes before tensor memory is freed
-                volatile int none = 0;
-                mbar_init(drain, 1);
-                asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-                umma_commit_one<kPair>(drain);
-                (void)mbar_wait_until<false>(drain, 0u, &none, p.err, 100000000ull);
-            }
         }
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag) {
+        // a wait ran out, in whichever role: what this CTA has in flight ends before its memory is
+        // given back.  (Else the epilogue has waited for every MMA, and those for every copy.)
+        volatile int none = 0;
+        for (int i = issued > kStages ? issued - kStages : 0; i < issued && (rank == 0 || !kPair); ++i)
+            (void)mbar_wait_until<kCluster>(&full[i % kStages], (uint32_t)((i / kStages) & 1), &none, p.err,
+                                            100000000ull);
+        if (warp == kMmaWarp && (rank == 0 || !kPair) && elect_lane()) {
+            mbar_init(drain, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            umma_commit_one<kPair>(drain);
+            (void)mbar_wait_until<false>(drain, 0u, &none, p.err, 100000000ull);
+        }
+        __syncwarp();
+    }
     // No CTA's memory is touched by another any more: a pair waits for that; the partial rows of a
     // split tile have all arrived, unless a wait ran out somewhere
     if (kPair || (kSplit && *abort_flag)) cluster_sync();
