@@ -8,7 +8,7 @@
 // takes as it stands.
 //
 // Measured on one GB300: 8192 x 4096 bfloat16 values 18.7 us, float32 27.9 us (5.4 and 6.0 TB/s);
-// bound by the memory.  The same rows to 8 experts each 65 us for 337 MB, of which 270 MB are
+// bound by the memory.  The same rows to 8 experts each 63 us for 337 MB, of which 270 MB are
 // writes: a plain fill of as many bytes takes 74 us.
 
 #include <cuda_bf16.h>
@@ -171,66 +171,94 @@ f8_quantize_kernel(const T* __restrict__ X, int64_t M, int64_t K, const int32_t*
     }
 }
 
-// Gathers with repeated source rows: each source row is quantized once and written to every
-// output row that names it.  With 8 rows of each of 8192 tokens of 4096 bfloat16 values the
-// kernel above is bound by its arithmetic, done eight times (120 us; the bytes: 50 us).
-//  1. lists: next[r] = the previous head of rows[r]'s list, head[rows[r]] = r.  The order within
-//     a list depends on the order of the atomics; the outputs do not.
+// Gathers with repeated source rows: each source row is quantized once for up to 32 output rows
+// that name it.  With 8 rows of each of 8192 tokens of 4096 bfloat16 values the kernel above
+// is bound by its arithmetic, done eight times (120 us; the bytes: 50 us).
+//
+// Room for the output rows of a source row: half as many again as a source row has on average.
+// Those beyond it, and those of a row outside X, go on one list of their own and are
+// quantized one by one as above: whatever the indexes are, no warp has more than 32 rows
+// (2^18 rows of one of 4000 sources: 0.10 ms, walked as one list 29 ms).
+struct Lists {
+    int32_t* count;   // [M] output rows that name the source row, [1] rows on `alone`
+    int32_t* slots;   // [M][cap] the first of them
+    int32_t* alone;   // [R]
+    int cap;
+};
+__host__ __device__ __forceinline__ int64_t list_cap(int64_t M, int64_t R) {
+    const int64_t each = (R + M - 1) / M;
+    return each + (each + 1) / 2;
+}
+//  1. Which row takes which place depends on the order of the atomics; the outputs do not.  Lanes
+//     that name the same source share an atomic.
 __global__ void __launch_bounds__(256)
-f8_list_kernel(const int32_t* __restrict__ rows, int64_t M, int64_t R, int32_t* __restrict__ head,
-               int32_t* __restrict__ next, uint8_t* __restrict__ codes, uint32_t* __restrict__ scales, int groups,
-               int quads) {
+f8_list_kernel(const int32_t* __restrict__ rows, int64_t M, int64_t R, Lists l) {
     pdl_trigger();
     pdl_wait();
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const int lane = threadIdx.x & 31;
+    const uint32_t below = (1u << lane) - 1u;
     const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (r >= R) return;
-    const int32_t src = __ldg(rows + r);
-    if (src >= 0 && src < M) {
-        next[r] = atomicExch(head + src, (int32_t)r);
-        return;
-    }
-    for (int64_t i = 0; i < (int64_t)groups * (kGroup / 16); ++i)   // a row outside X becomes a NaN row
-        reinterpret_cast<uint4*>(codes + r * groups * kGroup)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int q = 0; q < quads; ++q) {
-        uint32_t word = 0;
-        for (int j = 0; j < 4; ++j) word |= (4 * q + j < groups ? kF8NaN : kF8One) << (8 * j);
-        scales[r * quads + q] = word;
-    }
+    const int32_t src = r < R ? __ldg(rows + r) : -1;
+    const bool inside = src >= 0 && src < M;
+    const uint32_t peers = __match_any_sync(kAll, inside ? src : -1);
+    const int first = __ffs(peers) - 1;
+    int at = 0;
+    if (inside && lane == first) at = atomicAdd(l.count + src, __popc(peers));
+    at = __shfl_sync(kAll, at, first) + __popc(peers & below);
+    const bool listed = inside && at < l.cap;
+    if (listed) l.slots[(int64_t)src * l.cap + at] = (int32_t)r;
+    const bool alone = r < R && !listed;
+    const uint32_t who = __ballot_sync(kAll, alone);
+    if (!who) return;
+    int base = 0;
+    if (lane == 0) base = atomicAdd(l.count + M, __popc(who));
+    base = __shfl_sync(kAll, base, 0);
+    if (alone) l.alone[base + __popc(who & below)] = (int32_t)r;
 }
-//  2. A warp takes up to `per` quads of a source row and the row's list, 32 output rows at a time.
+//  2. A warp takes up to `per` quads of a source row for up to 32 rows of its list (`parts` of
+//     them), or of the source of one row of `alone`.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, kQuantCtas)
-f8_quantize_lists_kernel(const T* __restrict__ X, int64_t M, int64_t K, const int32_t* __restrict__ head,
-                         const int32_t* __restrict__ next_of, uint8_t* __restrict__ codes,
-                         uint32_t* __restrict__ scales, int quads, int per, int segs) {
+f8_quantize_lists_kernel(const T* __restrict__ X, int64_t M, int64_t K, const int32_t* __restrict__ rows, Lists l,
+                         uint8_t* __restrict__ codes, uint32_t* __restrict__ scales, int quads, int per, int segs,
+                         int parts) {
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const int groups = (int)((K + kGroup - 1) / kGroup);
-    const int64_t units = M * segs, warps = (int64_t)gridDim.x * 8;
+    const int64_t listed = M * parts, units = (listed + l.count[M]) * segs, warps = (int64_t)gridDim.x * 8;
     for (int64_t u = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5; u < units; u += warps) {
-        const int64_t src = segs == 1 ? u : u / segs;
-        const int q0 = (int)(u - src * segs) * per, q1 = min(q0 + per, quads);
-        const T* x = X + src * K;
-        for (int32_t r = head[src]; r >= 0;) {
-            Values16<T> v, next;
-            load16<VEC>(next, x, (int64_t)q0 * (4 * kGroup) + 16 * lane, K);
-            int32_t mine = 0;
-            int n = 0;
-            for (; n < 32 && r >= 0; ++n) {
-                if (lane == n) mine = r;
-                r = next_of[r];
-            }
-            for (int q = q0; q < q1; ++q) {
-                v = next;
-                if (q + 1 < q1) load16<VEC>(next, x, (int64_t)(q + 1) * (4 * kGroup) + 16 * lane, K);
-                const Quad d = quantize_quad(v, q, groups, lane, true);
-                for (int i = 0; i < n; ++i) {
-                    const int64_t to = __shfl_sync(0xffffffffu, mine, i);
-                    if (d.there)
-                        *reinterpret_cast<uint4*>(codes + (to * groups + 4 * q) * kGroup + 16 * lane) = d.codes;
-                }
-                if (lane < n) scales[(int64_t)mine * quads + q] = d.scales;
+        const int64_t w = segs == 1 ? u : u / segs;
+        const int q0 = (int)(u - w * segs) * per, q1 = min(q0 + per, quads);
+        int64_t src;
+        int32_t mine = 0;   // the output row of lane 0 .. n - 1
+        int n = 1;
+        bool inside = true;
+        if (w < listed) {
+            src = parts == 1 ? w : w / parts;
+            const int i0 = (int)(w - src * parts) * 32;
+            n = min(min(l.count[src], l.cap) - i0, 32);
+            if (n <= 0) continue;
+            if (lane < n) mine = l.slots[src * l.cap + i0 + lane];
+        } else {
+            mine = l.alone[w - listed];
+            src = __ldg(rows + mine);
+            inside = src >= 0 && src < M;   // a row outside X becomes a NaN row
+        }
+        const T* x = X + (inside ? src * K : 0);
+        const int64_t cols = inside ? K : 0;
+        Values16<T> v, next;
+        load16<VEC>(next, x, (int64_t)q0 * (4 * kGroup) + 16 * lane, cols);
+        for (int q = q0; q < q1; ++q) {
+            v = next;
+            if (q + 1 < q1) load16<VEC>(next, x, (int64_t)(q + 1) * (4 * kGroup) + 16 * lane, cols);
+            const Quad d = quantize_quad(v, q, groups, lane, inside);
+            if (lane < n) scales[(int64_t)mine * quads + q] = d.scales;
+            for (int i = 0; i < n; ++i) {
+                const int64_t to = __shfl_sync(0xffffffffu, mine, i);
+                if (d.there)   // streamed: 8192 x 4096 bfloat16 to 8 experts 62.8 us, 65.3 otherwise
+                    __stcs(reinterpret_cast<uint4*>(codes + (to * groups + 4 * q) * kGroup + 16 * lane), d.codes);
             }
         }
     }
@@ -296,7 +324,8 @@ static bool f8_use_lists(int64_t M, int64_t K, int64_t R) { return R >= 2 * M &&
 
 extern "C" size_t f8_quantize_workspace_bytes(int64_t M, int64_t K, int64_t R) {
     if (M < 1 || K < 1 || R < 1 || M > CQ_F8_MAX_ROWS || K > CQ_F8_MAX_K || R > CQ_F8_MAX_ROWS) return 0;
-    return f8_use_lists(M, K, R) ? (((size_t)M + (size_t)R) * sizeof(int32_t) + 255u) & ~(size_t)255u : 0;
+    if (!f8_use_lists(M, K, R)) return 0;
+    return (((size_t)M * (size_t)(1 + list_cap(M, R)) + 1u + (size_t)R) * sizeof(int32_t) + 255u) & ~(size_t)255u;
 }
 
 extern "C" cq_status f8_quantize(const void* X, cq_dtype xt, int64_t M, int64_t K, const int32_t* rows,
@@ -314,25 +343,31 @@ extern "C" cq_status f8_quantize(const void* X, cq_dtype xt, int64_t M, int64_t 
     if (space && (!workspace || workspace_bytes < space)) return CQ_ERR_WORKSPACE;
     const cudaStream_t cs = as_stream(stream);
     uint32_t* words = reinterpret_cast<uint32_t*>(scales);
-    int32_t* head = static_cast<int32_t*>(workspace);
-    int32_t* next = head + M;
+    Lists l = {};
+    int64_t from = R;   // pieces of work of a row each, at most
+    int parts = 1;
     if (space) {
-        const cudaError_t e = cudaMemsetAsync(head, 0xFF, (size_t)M * sizeof(int32_t), cs);   // -1: empty
+        l.cap = (int)list_cap(M, R);
+        l.count = static_cast<int32_t*>(workspace);
+        l.slots = l.count + M + 1;
+        l.alone = l.slots + M * l.cap;
+        parts = (l.cap + 31) / 32;
+        from = M * parts;
+        const cudaError_t e = cudaMemsetAsync(l.count, 0, ((size_t)M + 1) * sizeof(int32_t), cs);
         if (e != cudaSuccess) { set_last_cuda_error((int)e); return CQ_ERR_CUDA; }
-        const cq_status st = launch_pdl(f8_list_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, cs, rows, M, R,
-                                        head, next, codes, words, groups, quads);
+        const cq_status st = launch_pdl(f8_list_kernel, dim3((unsigned)((R + 255) / 256)), dim3(256), 0, cs, rows, M, R, l);
         if (st != CQ_OK) return st;
     }
     // whole rows where they give every warp several, else as many segments as fill the warps
-    const int64_t fill = (int64_t)sm_count() * kQuantCtas * 8, from = space ? M : R, want = space ? 4 * fill : fill;
+    const int64_t fill = (int64_t)sm_count() * kQuantCtas * 8, want = space ? 4 * fill : fill;
     int64_t segs64 = from >= want ? 1 : (want + from - 1) / from;
     if (segs64 > quads) segs64 = quads;
     const int per = (quads + (int)segs64 - 1) / (int)segs64;
     const int segs = (quads + per - 1) / per;
-    const int64_t need = (from * segs + 7) / 8;
+    const int64_t need = ((from > R ? from : R) * segs + 7) / 8;
     const dim3 gd((unsigned)(need < fill / 8 ? need : fill / 8)), bd(256);
     auto launch = [&](auto direct, auto lists, auto x) {
-        return space ? launch_pdl(lists, gd, bd, 0, cs, x, M, K, head, next, codes, words, quads, per, segs)
+        return space ? launch_pdl(lists, gd, bd, 0, cs, x, M, K, rows, l, codes, words, quads, per, segs, parts)
                      : launch_pdl(direct, gd, bd, 0, cs, x, M, K, rows, R, codes, words, quads, per, segs);
     };
     using bf16 = __nv_bfloat16;

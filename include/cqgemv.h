@@ -401,7 +401,8 @@ typedef enum cq_act {
  *   codes  [R][Kp], scales [R][Ks]
  *   workspace  with rows: >= f8_quantize_workspace_bytes(M, K, R) bytes (0: may be NULL).  Large
  *          gathers whose rows repeat (R >= 2 M) list the output rows of each source row there,
- *          so that every source row is read and quantized once
+ *          so that a source row is quantized once for up to 32 of them; rows that repeat far
+ *          more than others, and indexes outside X, are quantized one by one
  * All pointers 16-byte aligned.
  * Errors: INVALID_ARG (NULL, M, K or R < 1, R != M without rows, xt), UNSUPPORTED (K above
  * CQ_F8_MAX_K, M or R above CQ_F8_MAX_ROWS, more than 2^34 units of a row x 512 columns),
