@@ -351,19 +351,23 @@ __device__ __forceinline__ float rcp_approx(float x) {   // 1 ulp; 0 for infinit
     asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// g / (1 + exp(-g)) * u.  exp(-g) = 2^t (1 + lo ln 2) with t + lo = -g log2(e), so the rounding
-// of t does not grow with |g|; beyond 87 the exponential stays finite and the result is far
-// below one unit of u's last place (or g itself).  A few units of the last place in all,
-// in 11 instructions (expf and a division: four times the cycles of the store step).
+// g / (1 + exp(-g)) * u, with h = exp(-|g| / 2):  g u / (1 + h^2) for g >= 0, (g h) (u h) / (1 + h^2)
+// below.  The square root keeps h a normal number down to g = -174, where h^2 no longer is, so
+// that a result that a large u makes a normal number is right; from there on h = 0, an error
+// of at most 2^-240 |u|.  h = 2^-t with t + lo = |g| / 2 log2(e), log2(e) in two pieces, so the
+// rounding of t does not grow with |g|.  Within 17 * 2^-24 of the result: h twice (ex2 4, the
+// product 1), rcp 2, and five roundings.  g = -infinity gives NaN, as the formula does.
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-    const float c = fminf(fmaxf(g, -87.0f), 87.0f);
-    const float t = -kLog2e * c;
-    const float lo = fmaf(-kLog2e, c, -t);
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = fmaf(e, lo * kLn2, e);
-    return g * rcp_approx(1.0f + e) * u;
+    constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453;
+    constexpr float kHi = (float)(0.5 * kLog2e), kLo = (float)(0.5 * kLog2e - (double)kHi);
+    const float c = fminf(fabsf(g), 1024.0f);   // h is 0 long before
+    const float t = kHi * c;
+    const float lo = fmaf(kLo, c, fmaf(kHi, c, -t));
+    float h;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(h) : "f"(-t));
+    h = fmaf(h, lo * (float)-kLn2, h);
+    const float w = g < 0.0f ? h : 1.0f;
+    return g * w * rcp_approx(fmaf(h, h, 1.0f)) * (u * w);
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
