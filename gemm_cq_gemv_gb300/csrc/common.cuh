@@ -65,6 +65,14 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 // pdl_trigger() once all its blocks are resident, so the next launch can begin early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
+// The last step of a kernel that writes weights, by every thread that stored some.  Products may
+// read weights ahead of their pdl_wait(), after nothing but the end of this kernel's blocks
+// (which do not call pdl_trigger()): its stores are performed for the whole device, and for
+// asynchronous copies, before a block ends.
+__device__ __forceinline__ void weights_written() {
+    __threadfence();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 
 // `cluster` CTAs of the grid form a cluster; 0: no cluster attribute.
 template <typename... Params, typename... Args>

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(kEncThreads) cq_encode_kernel(const EncodePara
         if (lane == 0) p.norms[gi] = f64_to_f16_bits_rne(nrm);
         __syncwarp();
     }
+    weights_written();
 }
 
 // ---------------------------------------------------------------------------------
@@ -294,6 +295,7 @@ q4_0_quantize_kernel(const float* __restrict__ W, int64_t N, int64_t K, int64_t 
         }
         o[1 + k] = (uint16_t)word;
     }
+    weights_written();
 }
 
 inline int blocks_for(int64_t work, int per_block, int cap) {

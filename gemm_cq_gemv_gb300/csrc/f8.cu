@@ -311,6 +311,7 @@ f8_quantize_weights_kernel(const T* __restrict__ W, int64_t N, int64_t K, int64_
                     e4m3x4(scaled(v[i][0], inv), scaled(v[i][1], inv), scaled(v[i][2], inv), scaled(v[i][3], inv));
         }
     }
+    weights_written();
 }
 
 }  // namespace

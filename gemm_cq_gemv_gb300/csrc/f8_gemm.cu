@@ -772,7 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1) f8_gemm_kernel(const __grid_const
             bool any = walk.next(t);
             int k = k0;
             if constexpr (!C::EXPERTS) {
-                // the first stages' weights do not depend on the kernel before this one
+                // the first stages' weights do not depend on the kernel before this one, but for one
+                // that ends with weights_written() (after the wait: 1x4096x4096 5.8 -> 6.1 us)
                 if (any)
                     for (; k < k1 && issued < kStages; ++k, ++issued) copy_w(t, k, issued);
                 pdl_wait();

@@ -25,10 +25,14 @@
  *  - Kernels are launched with programmatic dependent launch: a kernel may start while
  *    the one before it on the stream finishes, and waits for it before it reads that
  *    kernel's outputs.  The batch-1 GEMVs and f8_gemm start reading their weight codes before
- *    that wait, so weights must be complete when the kernel launched just before the product
- *    starts: true for weights written by cq_encode, q4_0_quantize or f8_quantize_weights (none
- *    releases its dependents early), by a copy, or by any kernel that does not trigger
- *    dependent launches itself.
+ *    that wait, as soon as the kernel launched just before the product has ended or released
+ *    its dependents; the kernels of this library but cq_encode, q4_0_quantize and
+ *    f8_quantize_weights release theirs at their start.  So weights must be in memory by then:
+ *      - cq_encode, q4_0_quantize and f8_quantize_weights may be called right before the
+ *        product (they end with a device-wide fence), and so may a copy;
+ *      - weights that another kernel has written need a synchronisation of the stream, a copy
+ *        or a kernel launched without programmatic stream serialisation (any kernel that is
+ *        not of this library's) between that kernel and the product.
  *  - Arguments are validated before anything is launched; a failed check returns an
  *    error status and launches nothing.
  *  - Row-major layouts; sizes are element counts unless named *_bytes.
