@@ -492,7 +492,8 @@ def q4_0_gemm(blocks, N, K, X, Y=None, workspace=None, stream=None):
 # time of a step: one look at each tensor, addresses as plain integers, the stream's address
 # without a Stream object, shapes worked out in place.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# absent from builds of torch without CUDA, where the package still imports
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
 _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
