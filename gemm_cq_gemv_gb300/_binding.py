@@ -493,7 +493,8 @@ def q4_0_gemm(blocks, N, K, X, Y=None, workspace=None, stream=None):
 # without a Stream object, shapes worked out in place.
 
 # absent from builds of torch without CUDA, where the package still imports
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
@@ -507,14 +508,35 @@ def f8_scale_bytes(K) -> int:
     return (K + 4 * F8_GROUP - 1) // (4 * F8_GROUP) * 4
 
 
-def _at(t, dtype, shape, name):
-    """Address of a contiguous CUDA tensor of this dtype and shape; raises for any other."""
+def _raw_stream(device):
+    """Address of the current stream of the device, which has to be the current one: the library
+    launches there.  With a single device there is nothing to compare, and no call to spend."""
+    global _raw_stream
+    if torch.cuda.device_count() == 1:
+        _raw_stream = _current_stream
+    elif _current_device() != device:
+        raise ValueError(f"the tensors are on CUDA device {device}, which is not the current one")
+    return _current_stream(device)
+
+
+def _device(t, name):
+    """Device of a tensor, which the call's other tensors have to share; raises for one of the host."""
+    device = t.get_device()
+    if device < 0:
+        _ptr(t, t.dtype, name)
+    return device
+
+
+def _at(t, dtype, shape, name, device):
+    """Address of a contiguous tensor of this dtype and shape on this device; raises for any other."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
     _ptr(t, dtype, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on CUDA device {device} like the call's other tensors, got {t.get_device()}")
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -548,24 +570,25 @@ def f8_quantize(X, rows=None, codes=None, scales=None, workspace=None, stream=No
     comes from X[rows[r]]."""
     xt = _float(X, "X")
     M, K = shape = _dims(X, "X", 2)
-    xp = _at(X, X.dtype, shape, "X")
+    dev = _device(X, "X")
+    xp = _at(X, X.dtype, shape, "X", dev)
     R, rp, wp, wn = M, None, None, 0
     if rows is not None:
         R, = shape = _dims(rows, "rows", 1)
-        rp = _at(rows, _I32, shape, "rows")
+        rp = _at(rows, _I32, shape, "rows", dev)
         if workspace is None and R * K >= 1 << 20:   # smaller gathers take none
             need = f8_quantize_workspace_bytes(M, K, R)
             workspace = _empty((need,), _U8, X.device, stream) if need else None
         if workspace is not None:
-            wp, wn = _ptr(workspace, _U8, "workspace"), workspace.numel()
+            wp, wn = _at(workspace, _U8, _dims(workspace, "workspace", 1), "workspace", dev), workspace.numel()
     cs, ss = (R, (K + 127) // 128 * 128), (R, (K + 511) // 512 * 4)
     if codes is None:
         codes = _empty(cs, _U8, X.device, stream)
     if scales is None:
         scales = _empty(ss, _U8, X.device, stream)
     status = (_lib or lib()).f8_quantize(
-        xp, xt, M, K, rp, R, _at(codes, _U8, cs, "codes"), _at(scales, _U8, ss, "scales"), wp, wn,
-        _raw_stream(X.get_device()) if stream is None else _stream(stream))
+        xp, xt, M, K, rp, R, _at(codes, _U8, cs, "codes", dev), _at(scales, _U8, ss, "scales", dev), wp, wn,
+        _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check("f8_quantize", status)
     return codes, scales
@@ -576,7 +599,8 @@ def f8_quantize_weights(W, codes=None, scales=None, stream=None):
     [.., ceil(N / 128), Ks]): e4m3 codes with one power-of-two scale per 128 x 128 block."""
     wt = _float(W, "W")
     shape = _dims(W, "W", 2, 3)
-    wp = _at(W, W.dtype, shape, "W")
+    dev = _device(W, "W")
+    wp = _at(W, W.dtype, shape, "W", dev)
     *lead, N, K = shape
     cs = (*lead, N, f8_row_bytes(K))
     ss = (*lead, (N + F8_GROUP - 1) // F8_GROUP, f8_scale_bytes(K))
@@ -585,8 +609,8 @@ def f8_quantize_weights(W, codes=None, scales=None, stream=None):
     if scales is None:
         scales = _empty(ss, _U8, W.device, stream)
     _check("f8_quantize_weights", lib().f8_quantize_weights(
-        wp, wt, lead[0] if lead else 1, N, K, _at(codes, _U8, cs, "codes"), _at(scales, _U8, ss, "scales"),
-        _raw_stream(W.get_device()) if stream is None else _stream(stream)))
+        wp, wt, lead[0] if lead else 1, N, K, _at(codes, _U8, cs, "codes", dev), _at(scales, _U8, ss, "scales", dev),
+        _raw_stream(dev) if stream is None else _stream(stream)))
     return codes, scales
 
 
@@ -603,15 +627,15 @@ def f8_gemm(wcodes, wscales, N, K, xcodes, xscales, act="none", Y=None, stream=N
     """Y [M, N] = x w^T of F8 rows and F8 weights (bfloat16 unless a float32 ``Y`` is passed).
     ``act="swiglu"``: Y [M, N / 2] = silu(gate) * up over interleaved weight rows (gate 2 j,
     up 2 j + 1)."""
-    a, M = _gated(act), _dims(xcodes, "xcodes", 2)[0]
+    a, M, dev = _gated(act), _dims(xcodes, "xcodes", 2)[0], _device(xcodes, "xcodes")
     Kp, Ks, shape = (K + 127) // 128 * 128, (K + 511) // 512 * 4, (M, N >> a)
     if Y is None:
         Y = _empty(shape, _BF16, xcodes.device, stream)
     yt = _float(Y, "Y")
     status = (_lib or lib()).f8_gemm(
-        _at(wcodes, _U8, (N, Kp), "wcodes"), _at(wscales, _U8, ((N + 127) // 128, Ks), "wscales"), N, K,
-        _at(xcodes, _U8, (M, Kp), "xcodes"), _at(xscales, _U8, (M, Ks), "xscales"), M, a, _at(Y, Y.dtype, shape, "Y"), yt,
-        _raw_stream(xcodes.get_device()) if stream is None else _stream(stream))
+        _at(wcodes, _U8, (N, Kp), "wcodes", dev), _at(wscales, _U8, ((N + 127) // 128, Ks), "wscales", dev), N, K,
+        _at(xcodes, _U8, (M, Kp), "xcodes", dev), _at(xscales, _U8, (M, Ks), "xscales", dev), M, a,
+        _at(Y, Y.dtype, shape, "Y", dev), yt, _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check("f8_gemm", status)
     return Y
@@ -620,16 +644,16 @@ def f8_gemm(wcodes, wscales, N, K, xcodes, xscales, act="none", Y=None, stream=N
 def f8_gemm_experts(wcodes, wscales, N, K, offsets, xcodes, xscales, act="none", Y=None, stream=None):
     """``f8_gemm`` for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 (int32
     [E + 1], on the device) times matrix e of wcodes [E, N, Kp]; Y [R, N] or [R, N / 2]."""
-    a, R = _gated(act), _dims(xcodes, "xcodes", 2)[0]
+    a, R, dev = _gated(act), _dims(xcodes, "xcodes", 2)[0], _device(xcodes, "xcodes")
     E = _dims(offsets, "offsets", 1)[0] - 1
     Kp, Ks, shape = (K + 127) // 128 * 128, (K + 511) // 512 * 4, (R, N >> a)
     if Y is None:
         Y = _empty(shape, _BF16, xcodes.device, stream)
     yt = _float(Y, "Y")
     status = (_lib or lib()).f8_gemm_experts(
-        _at(wcodes, _U8, (E, N, Kp), "wcodes"), _at(wscales, _U8, (E, (N + 127) // 128, Ks), "wscales"), E, N, K,
-        _at(offsets, _I32, (E + 1,), "offsets"), _at(xcodes, _U8, (R, Kp), "xcodes"), _at(xscales, _U8, (R, Ks), "xscales"),
-        R, a, _at(Y, Y.dtype, shape, "Y"), yt, _raw_stream(xcodes.get_device()) if stream is None else _stream(stream))
+        _at(wcodes, _U8, (E, N, Kp), "wcodes", dev), _at(wscales, _U8, (E, (N + 127) // 128, Ks), "wscales", dev), E, N, K,
+        _at(offsets, _I32, (E + 1,), "offsets", dev), _at(xcodes, _U8, (R, Kp), "xcodes", dev),
+        _at(xscales, _U8, (R, Ks), "xscales", dev), R, a, _at(Y, Y.dtype, shape, "Y", dev), yt, _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check("f8_gemm_experts", status)
     return Y
@@ -645,23 +669,24 @@ def moe_route(logits, k, normalize=True, workspace=None, stream=None):
     every row in expert order (for ``f8_quantize``), ``pos`` the row of every choice (for
     ``moe_combine``).  ``normalize``: the weights sum to 1 over the k chosen, else over E."""
     T, E = shape = _dims(logits, "logits", 2)
-    lp = _at(logits, _F32, shape, "logits")
+    dev = _device(logits, "logits")
+    lp = _at(logits, _F32, shape, "logits", dev)
     if stream is not None:
         with _on(stream, logits.device):
             return moe_route(logits, k, normalize, workspace)
-    dev, empty, l = logits.device, torch.empty, _lib or lib()
+    device, empty, l = logits.device, torch.empty, _lib or lib()
     wp, wn = None, 0
     if workspace is not None:
-        wp, wn = _ptr(workspace, _U8, "workspace"), workspace.numel()
+        wp, wn = _at(workspace, _U8, _dims(workspace, "workspace", 1), "workspace", dev), workspace.numel()
     elif T > MOE_ONE_LAUNCH:
         wn = l.moe_route_workspace_bytes(T, E)
-        workspace = empty((wn,), dtype=_U8, device=dev)
+        workspace = empty((wn,), dtype=_U8, device=device)
         wp = workspace.data_ptr()
-    ids, weights = empty((T, k), dtype=_I32, device=dev), empty((T, k), dtype=_F32, device=dev)
-    rows, offsets = empty((T * k,), dtype=_I32, device=dev), empty((E + 1,), dtype=_I32, device=dev)
-    pos = empty((T, k), dtype=_I32, device=dev)
+    ids, weights = empty((T, k), dtype=_I32, device=device), empty((T, k), dtype=_F32, device=device)
+    rows, offsets = empty((T * k,), dtype=_I32, device=device), empty((E + 1,), dtype=_I32, device=device)
+    pos = empty((T, k), dtype=_I32, device=device)
     status = l.moe_route(lp, T, E, k, 1 if normalize else 0, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
-                         rows.data_ptr(), pos.data_ptr(), wp, wn, _raw_stream(logits.get_device()))
+                         rows.data_ptr(), pos.data_ptr(), wp, wn, _raw_stream(dev))
     if status:
         _check("moe_route", status)
     return ids, weights, offsets, rows, pos
@@ -673,12 +698,13 @@ def moe_combine(Y, pos, weights, out=None, stream=None):
     yt = _float(Y, "Y")
     R, N = ys = _dims(Y, "Y", 2)
     T, k = ps = _dims(pos, "pos", 2)
+    dev = _device(Y, "Y")
     if out is None:
         out = _empty((T, N), Y.dtype, Y.device, stream)
     ot = _float(out, "out")
     status = (_lib or lib()).moe_combine(
-        _at(Y, Y.dtype, ys, "Y"), yt, R, N, _at(pos, _I32, ps, "pos"), _at(weights, _F32, ps, "weights"), T, k,
-        _at(out, out.dtype, (T, N), "out"), ot, _raw_stream(Y.get_device()) if stream is None else _stream(stream))
+        _at(Y, Y.dtype, ys, "Y", dev), yt, R, N, _at(pos, _I32, ps, "pos", dev), _at(weights, _F32, ps, "weights", dev), T, k,
+        _at(out, out.dtype, (T, N), "out", dev), ot, _raw_stream(dev) if stream is None else _stream(stream))
     if status:
         _check("moe_combine", status)
     return out
