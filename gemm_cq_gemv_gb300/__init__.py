@@ -18,7 +18,7 @@ from ._binding import (CQError, CQ_TERNARY, LIB_PATH, NOALLOC_MAX_ELEMS, SIGNATU
                        make_gemv_layer, make_q4_0_layer, cq_gemv_layer, q4_0_gemv_layer,
                        LAYER_MAX_PROBLEMS, LAYER_MAX_K, F8_GROUP, MOE_MAX_EXPERTS, MOE_MAX_K, f8_row_bytes,
                        f8_scale_bytes, f8_quantize, f8_quantize_workspace_bytes, f8_quantize_weights,
-                       f8_gemm, f8_gemm_experts,
+                       f8_gemm, f8_gemm_experts, f8_gemm_plan,
                        moe_route, moe_route_workspace_bytes, moe_combine)
 
 __all__ = ["CQError", "CQ_TERNARY", "LIB_PATH", "NOALLOC_MAX_ELEMS", "SIGNATURES", "a8_quantize", "cq_abi_version", "cq_codebook",
@@ -31,5 +31,5 @@ __all__ = ["CQError", "CQ_TERNARY", "LIB_PATH", "NOALLOC_MAX_ELEMS", "SIGNATURES
            "q4_0_gemv_problem", "make_gemv_layer", "make_q4_0_layer", "cq_gemv_layer",
            "q4_0_gemv_layer", "LAYER_MAX_PROBLEMS", "LAYER_MAX_K", "F8_GROUP", "MOE_MAX_EXPERTS",
            "MOE_MAX_K", "f8_row_bytes", "f8_scale_bytes", "f8_quantize",
-           "f8_quantize_workspace_bytes", "f8_quantize_weights", "f8_gemm",
+           "f8_quantize_workspace_bytes", "f8_quantize_weights", "f8_gemm", "f8_gemm_plan",
            "f8_gemm_experts", "moe_route", "moe_route_workspace_bytes", "moe_combine"]

@@ -107,6 +107,7 @@ SIGNATURES = {
     "f8_quantize_weights": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _P, _P]),
     "f8_gemm": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _INT, _P, _INT, _P]),
     "f8_gemm_experts": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P, _P, _I64, _INT, _P, _INT, _P]),
+    "f8_gemm_plan": (_INT, [_I64, _I64, _I64, _I64, _INT, _INT, _P]),
     "moe_route_workspace_bytes": (_SZ, [_I64, _I64]),
     "moe_route": (_INT, [_P, _I64, _I64, _INT, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_combine": (_INT, [_P, _INT, _I64, _I64, _P, _P, _I64, _INT, _P, _INT, _P]),
@@ -657,6 +658,14 @@ def f8_gemm_experts(wcodes, wscales, N, K, offsets, xcodes, xscales, act="none",
     if status:
         _check("f8_gemm_experts", status)
     return Y
+
+
+def f8_gemm_plan(N, K, R, experts=0, act="none", dtype=torch.bfloat16):
+    """How ``f8_gemm`` (or ``f8_gemm_experts`` with this many experts) cuts a call of R rows: (tokens of
+    a tile at most, CTAs that share its weight rows, CTAs that share it along K)."""
+    plan = (ctypes.c_int32 * 3)()
+    _check("f8_gemm_plan", lib().f8_gemm_plan(experts, N, K, R, _gated(act), {_F32: 0, _BF16: 1}[dtype], plan))
+    return tuple(plan)
 
 
 def moe_route_workspace_bytes(T, E) -> int:

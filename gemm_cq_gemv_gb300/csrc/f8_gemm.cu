@@ -1068,10 +1068,12 @@ int f8_least_split(const F8Args& a) {
     return S;
 }
 
-// How a call is cut: tokens per tile, CTAs per tile along K, and the cycles that takes.
+// How a call is cut: tokens per tile, CTAs per tile along K, pairs of CTAs or single ones, and the
+// cycles that takes.
 struct F8Plan {
     int64_t cycles = INT64_MAX;
     int bt = 0, split = 1;
+    bool pairs = false;
 };
 
 // Cycles that the epilogue of a tile of h rows takes.
@@ -1124,6 +1126,7 @@ F8Plan f8_pair_plan(const F8Args& a) {
     const int64_t tn = (a.N + 2 * kRows - 1) / (2 * kRows), fit = f8_fit(2);
     F8Plan best;
     if (fit < 1) return best;
+    best.pairs = true;
     const int64_t tm0 = (a.R + 255) / 256;
     for (int64_t tm = tm0; tm < tm0 + 8; ++tm) {
         const int64_t h = ((a.R + tm - 1) / tm + 15) / 16 * 16;
@@ -1137,18 +1140,80 @@ F8Plan f8_pair_plan(const F8Args& a) {
     return best;
 }
 
+// Tokens per tile.  Measured in a graph, us, weights in turn beyond the L2 cache:
+//   N x K        M     16     32     64    128   pairs
+//   8192 x 8192  1   13.3   13.5   14.0   15.0   21.0
+//                32  14.3   13.6   13.7   15.4   17.2
+//                128 44.7   24.9   15.9   18.2   18.5
+//                192    -      -   24.2   17.9   19.2
+//                384    -      -   38.9   35.4   23.5
+//   4096 x 4096  129    -      -    9.1    9.8   10.9
+//                384    -      -   15.3   11.1   12.0
+//   11008 x 4096 128    -      -   20.2   12.5      -
+//   28672 x 8192 64     -   40.9   39.3   43.4   43.0
+//                128    -      -   44.7   46.5   45.2
+//                192    -      -      -   50.9   47.7
+// A wider tile has a shallower ring of weights and a longer epilogue; narrower ones are more,
+// down to where they no longer fit the SMs at once.  The fewest estimated cycles win.
+F8Plan f8_dense_plan(const F8Args& a) {
+    const int64_t tn = (a.N + kRows - 1) / kRows;
+    F8Plan best;
+    best.split = f8_least_split(a);
+    if (best.split == 1 && a.R > 64) best = f8_pair_plan(a);   // 28672 x 8192, 64 tokens: 43.0 us, single CTAs 39.3
+    for (int bt = 16; bt <= 128; bt *= 2) {
+        const F8Plan plan = f8_narrow_plan(a, bt, std::min<int64_t>(bt, (a.R + 15) / 16 * 16), (a.R + bt - 1) / bt * tn);
+        if (plan.cycles < best.cycles) best = plan;
+    }
+    return best;
+}
+
+// Tokens per tile, by the rows an expert has on average.  Measured in a graph, us, 32 experts of
+// 4096 x 4096 of uneven popularity:
+//   rows each    32     64    128   pairs
+//   1          55.8   55.6   57.7   61.2
+//   4          76.9   77.6   80.4   84.0
+//   32         90.6   87.4   86.2   90.0
+//   48         96.8   87.2   87.7   90.7
+//   96          149    106   95.6   97.3
+//   128         193    120    101   99.8
+//   192         264    158    124    111
+// and 8 experts of 1092 x 1544: 75 rows each 9.4, 7.0, 7.7, 9.8; 384 rows 21.7, 16.4, 11.8, 15.9.
+// The fewest estimated cycles win.  The offsets are on the device: the number of tiles is
+// estimated, half a tile lost per expert.
+F8Plan f8_experts_plan(const F8Args& a) {
+    const int64_t used = a.R < a.E ? a.R : a.E;   // experts that have rows, at most
+    const auto tiles = [&](int64_t bt, int64_t n) { return (a.N + n - 1) / n * std::max(used, a.R / bt + used / 2); };
+    const int64_t fit = f8_fit(2);
+    F8Plan best;
+    best.split = f8_least_split(a);
+    best.pairs = best.split == 1 && fit > 0;
+    best.bt = 224;
+    if (best.pairs) best.cycles = f8_pair_cycles(a, best.bt, tiles(best.bt, 2 * kRows), fit);
+    for (int bt = 32; bt <= 128; bt *= 2) {
+        const F8Plan plan = f8_narrow_plan(a, bt, bt, tiles(bt, kRows));
+        if (plan.cycles < best.cycles) best = plan;
+    }
+    return best;
+}
+
 template <int BT, bool EXPERTS>
 cq_status f8_narrow(const F8Args& a, int split) {
     return split > 1 ? f8_launch<F8Cfg<BT, EXPERTS, false, true>>(a, split) : f8_launch<F8Cfg<BT, EXPERTS>>(a, 1);
 }
 
-cq_status f8_check(const F8Args& a) {
-    if (!a.wc || !a.ws || !a.xc || !a.xs || !a.Y) return CQ_ERR_INVALID_ARG;
+cq_status f8_check_sizes(const F8Args& a) {
     if (a.E < 1 || a.N < 1 || a.K < 1 || a.R < 1 || !cq_dtype_valid(a.yt)) return CQ_ERR_INVALID_ARG;
     if (a.act != CQ_ACT_NONE && a.act != CQ_ACT_SWIGLU) return CQ_ERR_INVALID_ARG;
     if (a.act == CQ_ACT_SWIGLU && a.N % 2 != 0) return CQ_ERR_INVALID_ARG;
     if (a.E > CQ_MOE_MAX_EXPERTS || a.N > CQ_F8_MAX_N || a.K > CQ_F8_MAX_K || a.R > CQ_F8_MAX_ROWS)
         return CQ_ERR_UNSUPPORTED;
+    return f8_tiles(a, 16, 1) > (1 << 30) ? CQ_ERR_UNSUPPORTED : CQ_OK;   // 32-bit tile numbers
+}
+
+cq_status f8_check(const F8Args& a) {
+    if (!a.wc || !a.ws || !a.xc || !a.xs || !a.Y) return CQ_ERR_INVALID_ARG;
+    const cq_status st = f8_check_sizes(a);
+    if (st != CQ_OK) return st;
     if (!aligned16(a.wc) || !aligned16(a.ws) || !aligned16(a.xc) || !aligned16(a.xs) || !aligned16(a.Y))
         return CQ_ERR_ALIGNMENT;
     return CQ_OK;
@@ -1192,34 +1257,10 @@ extern "C" cq_status f8_gemm(const uint8_t* wcodes, const uint8_t* wscales, int6
     const F8Args a = {wcodes, wscales, xcodes, xscales, nullptr, 1, N, K, M, act, Y, yt, as_stream(stream)};
     unsigned int* err = nullptr;
     cq_status st = f8_check(a);
-    if (st == CQ_OK && f8_tiles(a, 16, 1) > (1 << 30)) st = CQ_ERR_UNSUPPORTED;   // 32-bit tile numbers
     if (st == CQ_OK) st = f8_setup(&err);
     if (st != CQ_OK) return st;
-    // Tokens per tile.  Measured in a graph, us, weights in turn beyond the L2 cache:
-    //   N x K        M     16     32     64    128   pairs
-    //   8192 x 8192  1   13.3   13.5   14.0   15.0   21.0
-    //                32  14.3   13.6   13.7   15.4   17.2
-    //                128 44.7   24.9   15.9   18.2   18.5
-    //                192    -      -   24.2   17.9   19.2
-    //                384    -      -   38.9   35.4   23.5
-    //   4096 x 4096  129    -      -    9.1    9.8   10.9
-    //                384    -      -   15.3   11.1   12.0
-    //   11008 x 4096 128    -      -   20.2   12.5      -
-    //   28672 x 8192 64     -   40.9   39.3   43.4   43.0
-    //                128    -      -   44.7   46.5   45.2
-    //                192    -      -      -   50.9   47.7
-    // A wider tile has a shallower ring of weights and a longer epilogue; narrower ones are more,
-    // down to where they no longer fit the SMs at once.  The fewest estimated cycles win.
-    const int64_t tn = (N + kRows - 1) / kRows;
-    F8Plan best;
-    best.split = f8_least_split(a);
-    if (best.split == 1 && M > 64) best = f8_pair_plan(a);   // 28672 x 8192, 64 tokens: 43.0 us, single CTAs 39.3
-    bool pairs = best.bt != 0;
-    for (int bt = 16; bt <= 128; bt *= 2) {
-        const F8Plan plan = f8_narrow_plan(a, bt, std::min<int64_t>(bt, (M + 15) / 16 * 16), (M + bt - 1) / bt * tn);
-        if (plan.cycles < best.cycles) best = plan, pairs = false;
-    }
-    if (pairs)
+    const F8Plan best = f8_dense_plan(a);
+    if (best.pairs)
         return best.bt > 224 ? f8_launch<F8Cfg<256, false, true>>(a, 1, best.bt)
                              : f8_launch<F8Cfg<224, false, true>>(a, 1, best.bt);
     switch (best.bt) {
@@ -1238,37 +1279,30 @@ extern "C" cq_status f8_gemm_experts(const uint8_t* wcodes, const uint8_t* wscal
     unsigned int* err = nullptr;
     cq_status st = f8_check(a);
     if (st == CQ_OK && !aligned16(offsets)) st = CQ_ERR_ALIGNMENT;
-    if (st == CQ_OK && f8_tiles(a, 16, 1) > (1 << 30)) st = CQ_ERR_UNSUPPORTED;
     if (st == CQ_OK) st = f8_setup(&err);
     if (st != CQ_OK) return st;
-    // Tokens per tile, by the rows an expert has on average.  Measured in a graph, us, 32 experts of
-    // 4096 x 4096 of uneven popularity:
-    //   rows each    32     64    128   pairs
-    //   1          55.8   55.6   57.7   61.2
-    //   4          76.9   77.6   80.4   84.0
-    //   32         90.6   87.4   86.2   90.0
-    //   48         96.8   87.2   87.7   90.7
-    //   96          149    106   95.6   97.3
-    //   128         193    120    101   99.8
-    //   192         264    158    124    111
-    // and 8 experts of 1092 x 1544: 75 rows each 9.4, 7.0, 7.7, 9.8; 384 rows 21.7, 16.4, 11.8, 15.9.
-    // The fewest estimated cycles win.  The offsets are on the device: the number of tiles is
-    // estimated, half a tile lost per expert.
-    const int64_t used = R < E ? R : E;   // experts that have rows, at most
-    const auto tiles = [&](int64_t bt, int64_t n) { return (N + n - 1) / n * std::max(used, R / bt + used / 2); };
-    const int64_t fit = f8_fit(2);
-    F8Plan best;
-    best.split = f8_least_split(a);
-    bool pairs = best.split == 1 && fit > 0;
-    if (pairs) best.cycles = f8_pair_cycles(a, 224, tiles(224, 2 * kRows), fit);
-    for (int bt = 32; bt <= 128; bt *= 2) {
-        const F8Plan plan = f8_narrow_plan(a, bt, bt, tiles(bt, kRows));
-        if (plan.cycles < best.cycles) best = plan, pairs = false;
-    }
-    if (pairs) return f8_launch<F8Cfg<224, true, true>>(a, 1);
+    const F8Plan best = f8_experts_plan(a);
+    if (best.pairs) return f8_launch<F8Cfg<224, true, true>>(a, 1);
     switch (best.bt) {
         case 32: return f8_narrow<32, true>(a, best.split);
         case 64: return f8_narrow<64, true>(a, best.split);
         default: return f8_narrow<128, true>(a, best.split);
     }
+}
+
+extern "C" cq_status f8_gemm_plan(int64_t E, int64_t N, int64_t K, int64_t R, cq_act act, cq_dtype yt, int32_t* plan) {
+    if (!plan || E < 0) return CQ_ERR_INVALID_ARG;
+    F8Args a = {};
+    a.offsets = E ? plan : nullptr;   // experts or not; not read
+    a.E = E ? E : 1;
+    a.N = N; a.K = K; a.R = R; a.act = act; a.yt = yt;
+    unsigned int* err = nullptr;
+    cq_status st = f8_check_sizes(a);
+    if (st == CQ_OK) st = f8_setup(&err);
+    if (st != CQ_OK) return st;
+    const F8Plan best = E ? f8_experts_plan(a) : f8_dense_plan(a);
+    plan[0] = best.bt;
+    plan[1] = best.pairs ? 2 : 1;
+    plan[2] = best.split;
+    return CQ_OK;
 }

@@ -455,6 +455,13 @@ cq_status f8_gemm_experts(const uint8_t* wcodes, const uint8_t* wscales, int64_t
                           const uint8_t* xscales, int64_t R, cq_act act, void* Y, cq_dtype yt,
                           void* stream);
 
+/* How f8_gemm (E = 0, R tokens) or f8_gemm_experts (E matrices, R rows) cuts a call on the current
+ * device: plan[0] the tokens of a tile at most, plan[1] the CTAs that share a tile's weight rows (2:
+ * pairs, 256 rows; 1: 128 rows), plan[2] the CTAs that share a tile along K.  Launches nothing.
+ * Errors: as those calls for the same sizes. */
+cq_status f8_gemm_plan(int64_t E, int64_t N, int64_t K, int64_t R, cq_act act, cq_dtype yt,
+                       int32_t* plan);
+
 /* Softmax top-k routing of T tokens over E experts, and the order of the T k rows by expert.
  *   logits  [T][E] float32.  -infinity masks an expert; NaN counts as -infinity.
  *   ids     [T][k] int32: the k largest logits, descending; equal ones by lowest expert
