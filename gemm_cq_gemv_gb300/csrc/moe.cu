@@ -471,7 +471,8 @@ cq_status launch_combine(const void* Y, int64_t R, int64_t N, const int32_t* pos
 using namespace cq;
 
 // Tokens per CTA of the selection: one for every warp, as long as a cluster (or two CTAs per
-// SM, beyond a cluster's worth of tokens) holds them all, else what makes that many CTAs.
+// SM, beyond a cluster's worth of tokens) holds them all, else what makes that many CTAs.  152
+// SMs as a constant: the workspace's size must not depend on the current device.
 static int route_chunk(int64_t T) {
     const int64_t ctas = T <= CQ_MOE_ONE_LAUNCH ? kMaxCluster : 2 * 152;
     const int64_t even = (T + ctas - 1) / ctas;
