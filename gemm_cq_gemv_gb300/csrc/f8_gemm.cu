@@ -36,8 +36,10 @@
 //                matrices are bound by the launch and one pipeline fill: 1x4096x4096 5.2 us.
 //   many tokens  the power limit: 2048x28672x8192 with N(0,1) operands runs at 3.5 PFLOP/s for the
 //                first milliseconds and 3.0 to 3.1 at the 1.4 to 1.5 GHz that 1400 W leave
-//                (bf16 library product, same shape: 2.0 and 1.7).  At a given clock the shared
-//                memory binds: a stage of 224 rows takes 480 cycles, 448 of them tensor work.
+//                (bf16 library product, same shape: 2.0 and 1.7): 0.86 to 0.89 of the tensor rate
+//                at that clock (16384 operations a cycle and SM).  Calls at K = 8192 fit 256 + h
+//                cycles for a stage of h rows, of which the tensor work alone is 2 h: what is left
+//                at few rows is shared memory.
 
 #include <cuda_bf16.h>
 
@@ -1016,7 +1018,8 @@ int64_t f8_tiles(const F8Args& a, int BT, int rows) {
 // Runs of K with an accumulator of their own.  The tensor core cuts off what does not fit the
 // accumulator's 24 bits at each of its K / 32 additions, an error that grows with K: up to 1.1e-6 of
 // the result (2-norm) at K = 3300 and 3.7e-6 at 15000.  A float32 result keeps runs of at most
-// 2048 values apart and adds them with rounding, a bfloat16 one (2e-3) does not.  A gated one
+// 2048 values apart and adds them with rounding (2e-7 as a rule, at most 1e-6 in ten thousand random
+// cases; a float32 product 0.7e-7), a bfloat16 one (2e-3) does not.  A gated one
 // needs the whole sum before it is written: f8_least_split spreads its K over a cluster instead.
 constexpr int kRunGroups = 16, kGatedRunGroups = 20;   // groups of 128
 int f8_runs(const F8Args& a, int kb, int split) {
@@ -1109,11 +1112,12 @@ F8Plan f8_narrow_plan(const F8Args& a, int bt, int64_t h, int64_t tiles) {
     return best;
 }
 
-// Cycles of a call of pairs with tiles of h rows.  Measured at K = 8192: a stage takes 256 + h
-// cycles up to 224 rows (its four MMAs read, and its copies write, 64 + h / 4 cycles' worth of
-// shared memory each; the tensor work alone is 2 h).  256 rows take 484, and from tile to tile
-// 4000, in which the next one's MMAs wait for the shared columns (half of that for a single tile).
-// A call of pairs takes 6000 longer than one of CTAs, so that single CTAs win while one wave of
+// Cycles of a call of pairs with tiles of h rows: coefficients that fit the times of whole calls at
+// K = 8192 and order them rightly, not the times of single stages.  256 + h a stage up to 224 rows
+// (its four MMAs read, and its copies write, 64 + h / 4 cycles' worth of shared memory each; the
+// tensor work alone is 2 h).  Taller ones fit 228 + h (below the 512 of the tensor work at 256
+// rows) with 4000 from tile to tile, in which the next one's MMAs wait for the shared columns.
+// A call of pairs fits 6000 more than one of single CTAs, which therefore win while one wave of
 // them is enough: 8192 x 8192, 192 tokens, 17.9 us against 19.2; 384 tokens, 35.4 against 23.5.
 int64_t f8_pair_cycles(const F8Args& a, int64_t h, int64_t tiles, int64_t fit) {
     const int64_t kb = (a.K + kKB - 1) / kKB;
