@@ -509,15 +509,19 @@ def f8_scale_bytes(K) -> int:
     return (K + 4 * F8_GROUP - 1) // (4 * F8_GROUP) * 4
 
 
-def _raw_stream(device):
+def _checked_stream(device):
     """Address of the current stream of the device, which has to be the current one: the library
-    launches there.  With a single device there is nothing to compare, and no call to spend."""
-    global _raw_stream
-    if torch.cuda.device_count() == 1:
-        _raw_stream = _current_stream
-    elif _current_device() != device:
+    launches there."""
+    if _current_device() != device:
         raise ValueError(f"the tensors are on CUDA device {device}, which is not the current one")
     return _current_stream(device)
+
+
+def _raw_stream(device):
+    """``_checked_stream``; where there is a single device, without the call that the check takes."""
+    global _raw_stream
+    _raw_stream = _current_stream if torch.cuda.device_count() == 1 else _checked_stream
+    return _raw_stream(device)
 
 
 def _device(t, name):

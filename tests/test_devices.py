@@ -58,6 +58,7 @@ def calls(monkeypatch):
     monkeypatch.setattr(_binding, "_lib", c)
     monkeypatch.setattr(_binding, "_current_device", lambda: 0)
     monkeypatch.setattr(_binding, "_current_stream", lambda device: 0)
+    monkeypatch.setattr(_binding, "_raw_stream", _binding._checked_stream)   # as with several devices
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
     return c
 
